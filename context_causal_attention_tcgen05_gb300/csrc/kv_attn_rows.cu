@@ -3,14 +3,18 @@
 //
 // Mathematics as in kv_attn.cu; here the products bound, 4*D flops a (row, key) pair and
 // query head, so the queries are the M side and the products run in kind::f16: an e4m3
-// code times a power of two is exact in fp16 while it stays within 2^24 of the unit's
-// largest scale, q is scaled to [128, 256) a row (its 8 bits are exact), and the weights
-// keep 11 bits.  Codes are converted once per key tile and used by 256 rows.
+// code times a power of two down to 2^-15 is exact in fp16, so a page's scale relative to the
+// unit's largest goes into its converted codes; q is scaled to [128, 256) a row (its 8 bits are
+// exact down to 2^-25 of the row's largest), and the weights keep 11 bits.  Codes are converted
+// once per key tile and used by 256 rows.
+// A unit whose seen pages differ by more than kKeySpan or kValueSpan (`wide`) is rare and
+// would lose its small pages so: there the codes are converted as they are and the softmax
+// applies the scales in fp32 (wide_tile), which no row's accuracy depends on another's for.
 //
 // Two CTAs on neighbouring SMs work as a pair (cta_group::2): a product has 256 rows, 128 in
 // each CTA, and each CTA holds half of its B operand (64 of the tile's keys for S, half of the
 // head's columns for O).  So a code is converted once for 512 query rows, and an SM reads and
-// converts half a tile.  A chunk of 2048 rows over 32768 tokens, 32 heads: 0.855 ms, 1245 TFLOP/s
+// converts half a tile.  A chunk of 2048 rows over 32768 tokens, 32 heads: 0.831 ms, 1281 TFLOP/s
 // (one CTA a tile, with twice the conversion on each SM: 1.16 ms).
 //
 // One CTA an SM, 16 warps:
@@ -54,6 +58,12 @@ constexpr uint64_t kDrainNs = 200000000ull;
 // a score passes m + kLog2Range: weights stay under 2^15, and fp16's smallest step is 2^-31 of
 // the largest.
 constexpr float kLog2Unit = 7.0f, kLog2Range = 15.0f;
+// Least ratio of a unit's scales that goes into its codes: keys stay exact; values leave a row that
+// sees small ones beside large ones its weights to 2^-22 of its largest product.
+constexpr float kKeySpan = 0x1p-15f, kValueSpan = 0x1p-10f;
+// In a wide unit a row's reference goes down to this under its largest score, so that the weights of
+// values 2^-100 as large as the unit's largest still fill fp16's range (the sums stay under 2^127).
+constexpr int kWideLog2 = 100;
 
 template <int D>
 struct Layout {
@@ -71,9 +81,10 @@ struct Layout {
   static constexpr int kSmemRequest = kBytes > 120 * 1024 ? kBytes : 120 * 1024;  // one CTA an SM
 };
 
+constexpr int kBad = 1, kWide = 2;  // kWide: the codes are converted without their scales (k_ref is 1)
 struct Unit {
   int32_t b, hk, tile0, ntiles, len, n, nrows, c0, r0, part;
-  int32_t bad;          // some page of the unit does not exist: its tokens are hidden
+  int32_t special;      // kBad: some page of the unit does not exist (its tokens are hidden); kWide
   float k_ref, v_ref;   // largest key / value scale of the unit's pages
 };
 
@@ -279,7 +290,7 @@ __device__ __forceinline__ void hide(uint32_t (&s)[32], int ch, int ilo, int ihi
   const uint32_t kInf = 0xff800000u;
 #pragma unroll
   for (int i = 0; i < 32; ++i) s[i] = (ch * 32 + i >= ilo && ch * 32 + i < ihi) ? s[i] : kInf;
-  if (!un.bad) return;
+  if (!(un.special & kBad)) return;
 #pragma unroll
   for (int i = 0; i < 32; i += 16) {  // pages are multiples of 16 tokens
     const int key = key0 + ch * 32 + i;
@@ -289,6 +300,87 @@ __device__ __forceinline__ void hide(uint32_t (&s)[32], int ch, int ilo, int ihi
 #pragma unroll
     for (int k = 0; k < 16; ++k) s[i + k] = kInf;
   }
+}
+
+// One key tile of a wide unit, its scores in the warp's lanes of TMEM from `s_addr` on; the weights
+// are left there as the product wants them.  qs: factor of the row's scores without the keys' scales;
+// [ilo, ihi): the tile's tokens that the row sees; o_addr: the row's O, rescaled where `rescale`.
+// The reference m is chosen by the weights times their value scales (v_ref is the unit's largest), and
+// renewed in every tile.  Speed does not matter here; rolled loops keep the usual path's registers and
+// instruction cache.
+template <int D>
+__device__ __forceinline__ float2 wide_tile(const Unit& un, const CacheAttnArgs& a, uint32_t s_addr, uint32_t o_addr, float qs,
+                                         int ilo, int ihi, int key0, float m, float l, bool rescale) {
+  const float v_inv = 1.f / un.v_ref;
+  // key and value scale of the 16 tokens from column col on (pages are multiples of 16 tokens), the
+  // latter relative to v_ref; a token that some row sees has at most v_ref
+  auto scales = [&](int col) {
+    const int key = key0 + col;
+    if (key >= un.len) return make_float2(0.f, 0.f);
+    const int id = __ldg(a.page_table + (int64_t)un.b * a.max_pages + key / a.page);
+    if (id < 0 || id >= a.n_pages) return make_float2(0.f, 0.f);
+    const int64_t at = (int64_t)id * a.Hkv + un.hk;
+    const float f = __ldg(a.k_scale + at) * qs, v = __ldg(a.v_scale + at);
+    // (a score of 0 stays 0 where the factor alone passes fp32)
+    return make_float2(f > 3e38f ? 3e38f : f, v > 0.f ? fminf(v * v_inv, 1.f) : 0.f);
+  };
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int ch = 0; ch < BK / 32; ++ch) {
+    uint32_t s[32];
+    ptx::tmem_ld32(s_addr + ch * 32, s);
+    ptx::tmem_wait_ld_regs(s);
+#pragma unroll
+    for (int g = 0; g < 32; g += 16) {
+      const float2 f = scales(ch * 32 + g);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[g + i] = __float_as_uint(__uint_as_float(s[g + i]) * f.x);
+    }
+    hide(s, ch, ilo, ihi, key0, un, a);
+#pragma unroll
+    for (int g = 0; g < 32; g += 16) {
+      const int e = (int)(__float_as_uint(scales(ch * 32 + g).y) >> 23) - 127;
+      float mt = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mt = fmaxf(mt, __uint_as_float(s[g + i]));
+      top = fmaxf(top, mt + (float)max(e, -kWideLog2));
+    }
+    ptx::tmem_st32(s_addr + ch * 32, s);
+  }
+  const float m_new = fmaxf(m, top - kLog2Unit), alpha = m == -INFINITY ? 0.f : ptx::ex2_approx(m - m_new);
+  l *= alpha;
+  if (rescale) {
+#pragma unroll 1
+    for (int ch = 0; ch < D / 32; ++ch) {
+      uint32_t o[32];
+      ptx::tmem_ld32(o_addr + ch * 32, o);
+      ptx::tmem_wait_ld_regs(o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+      ptx::tmem_st32(o_addr + ch * 32, o);
+    }
+  }
+  ptx::tmem_wait_st();
+  const float ref = m_new == -INFINITY ? 0.f : m_new;
+#pragma unroll 1
+  for (int ch = 0; ch < BK / 32; ++ch) {  // the weights of 32 tokens take 16 columns, behind the scores read so far
+    uint32_t s[32], p[16];
+    ptx::tmem_ld32(s_addr + ch * 32, s);
+    ptx::tmem_wait_ld_regs(s);
+#pragma unroll
+    for (int g = 0; g < 32; g += 16) {
+      const float f = scales(ch * 32 + g).y;
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float p0 = ptx::ex2_approx(__uint_as_float(s[g + i]) - ref), p1 = ptx::ex2_approx(__uint_as_float(s[g + i + 1]) - ref);
+        l += p0 + p1;
+        p[(g + i) / 2] = pack_f16x2(p0 * f, p1 * f);
+      }
+    }
+    ptx::tmem_st16(s_addr + ch * 16, p);
+  }
+  ptx::tmem_wait_st();
+  return make_float2(m_new, l);
 }
 
 template <int D>
@@ -376,7 +468,7 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
           const int p0 = tile0 * ppt, p_end = min((tile0 + n) * ppt, (q.len + a.page - 1) / a.page);
           // the unit's largest scales, among the pages that some row sees: the others' tokens count as zeros
           const int seen0 = sr.lo / a.page, seen1 = (sr.hi + a.page - 1) / a.page;
-          float kr = 0.f, vr = 0.f;
+          float kr = 0.f, vr = 0.f, k_min = INFINITY, v_min = INFINITY;
           bool bad = false;
 #pragma unroll 4
           for (int p = p0 + lane; p < p_end; p += 32) {
@@ -385,13 +477,17 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
               record_device_error(a.err, kDevIndex);
               bad = true;
             } else if (p >= seen0 && p < seen1) {
-              kr = fmaxf(kr, __ldg(a.k_scale + (int64_t)id * a.Hkv + head));
-              vr = fmaxf(vr, __ldg(a.v_scale + (int64_t)id * a.Hkv + head));
+              const float k = __ldg(a.k_scale + (int64_t)id * a.Hkv + head), v = __ldg(a.v_scale + (int64_t)id * a.Hkv + head);
+              kr = fmaxf(kr, k);  // (NaN is none of these)
+              vr = fmaxf(vr, v);
+              k_min = fminf(k_min, k);
+              v_min = fminf(v_min, v);
             }
           }
           kr = fmaxf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(kr))), 1.17549435e-38f);
           vr = fmaxf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vr))), 1.17549435e-38f);
           bad = __any_sync(0xffffffffu, bad);
+          const bool wide = __any_sync(0xffffffffu, k_min < kr * kKeySpan || v_min < vr * kValueSpan);
           if (u >= 2) ok = wait(&ctl.u_empty[u & 1], (u >> 1) - 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -407,8 +503,8 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
             un.c0 = q.c0;
             un.r0 = sr.r0;
             un.part = n == t1 - t0 ? -1 : 2 * pair + (pc.k0 > 0 ? 0 : 1);
-            un.bad = bad;
-            un.k_ref = kr;
+            un.special = (bad ? kBad : 0) | (wide ? kWide : 0);
+            un.k_ref = wide ? 1.f : kr;
             un.v_ref = vr;
             if (pc.k0 == 0 && rank == 0)
               ws.info[(int64_t)slot * a.Hkv + head] =
@@ -417,7 +513,7 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
           }
           __syncwarp();
           // tiles: 32 pages at a time, their ids and factors one batch ahead
-          const float k_inv = 1.f / kr, v_inv = 1.f / vr;
+          const float k_inv = wide ? 0.f : 1.f / kr, v_inv = wide ? 0.f : 1.f / vr, one = wide ? 1.f : 0.f;
           int id, id_n;
           uint32_t kf, vf, kf_n, vf_n;
           auto fetch = [&](int p, int& i, uint32_t& k2, uint32_t& v2) {
@@ -429,8 +525,9 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
                 i = -1;
               } else if (p + lane >= seen0 && p + lane < seen1) {
                 const float k = __ldg(a.k_scale + (int64_t)i * a.Hkv + head), v = __ldg(a.v_scale + (int64_t)i * a.Hkv + head);
-                k2 = v != v ? 0x7e007e00u : pack_f16x2(k * k_inv, k * k_inv);  // a NaN scale reaches the scores
-                v2 = v != v ? 0u : pack_f16x2(v * v_inv, v * v_inv);
+                const float kf = fmaf(k, k_inv, one), vf = fmaf(v, v_inv, one);
+                k2 = v != v ? 0x7e007e00u : pack_f16x2(kf, kf);  // a NaN scale reaches the scores
+                v2 = v != v ? 0u : pack_f16x2(vf, vf);
               }
             }
           };
@@ -710,7 +807,15 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
         ok = __all_sync(0xffffffffu, wait(&ctl.s_full[w], c));
         if (!ok) break;
         ptx::tc_fence_after();
-        if (!(key0 >= lo_max && key0 + BK <= hi_min) || un.bad) {  // hidden scores become -inf in place
+        if (un.special & kWide) {
+          const float2 ml = wide_tile<D>(un, a, lane_addr, lane_addr + 128, sl2, lo - key0, hi - key0, key0, m, l, t > t_first);
+          m = ml.x;
+          l = ml.y;
+          ptx::tc_fence_before();
+          arrive_first(&ctl.p_full[w], lane);
+          continue;
+        }
+        if (!(key0 >= lo_max && key0 + BK <= hi_min) || un.special) {  // hidden scores become -inf in place
 #pragma unroll 1
           for (int ch = 0; ch < BK / 32; ++ch) {
             uint32_t rr[32];

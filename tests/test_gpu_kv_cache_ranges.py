@@ -1,0 +1,97 @@
+"""Attention over the key/value cache where the blocks' scales, the pages that are seen and the rows' lengths differ
+widely inside one call: every row keeps the accuracy of what it sees itself."""
+import numpy as np
+import pytest
+import torch
+
+import context_causal_attention_tcgen05_gb300 as cpa
+from gpu_common import _record, check_ok, need_gpu
+from oracle import serving
+from test_gpu_kv_cache import BF16, F32, Cache, i32, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def reference(c, b, q, L, pos_q, window=0, pos_k=None, k=None, v=None, v_scale=None):
+    """out, lse and their bounds for rows q [n, Hq, D] over the first L tokens of sequence b (or over k, v).
+
+    |s| is off by at most D + 8 fp32 roundings of its terms (sabs: the largest sum of their magnitudes) and a weight by
+    twice that, the exponential's 2^-21 and, for bf16, its rounding to 11 bits (2^-12); the sum over the keys and the
+    division by at most 2^-18; the result is rounded once.  A row's weights are kept in steps of 2^-22 (bf16; fp32 2^-28)
+    of its own largest product of a weight and a value scale, half a step off each, and a code is at most 448.  So a score
+    is taken relative to a reference that lies up to the spread of the value scales from the row's maximum; the
+    difference, at most that spread and 16 in powers of two, is rounded to fp32."""
+    bf16 = q.dtype == BF16
+    x = q.double().cpu().numpy()
+    k = c.values(0, b, L) if k is None else k
+    v = c.values(1, b, L) if v is None else v
+    pos_k = np.arange(L) if pos_k is None else pos_k
+    n, Hq, D = x.shape
+    G = Hq // k.shape[1]
+    ref, rl, absv, sabs = serving.cache_attention(x, k, v, pos_q, pos_k, True, window)
+    if v_scale is None:
+        v_scale = c.scales[1][[int(c.table[b][t // c.page]) for t in range(L)]].astype(np.float64)  # [L, Hkv]
+    see = pos_k[None] <= pos_q[:, None]
+    if window:
+        see &= pos_q[:, None] - pos_k[None] < window
+    top = np.zeros((n, Hq))
+    for h in range(Hq):
+        s = np.where(see, (x[:, h] @ k[:, h // G].T) * D**-0.5, -np.inf)
+        z = np.where(np.isfinite(rl[h]), rl[h], 0)[:, None]
+        top[:, h] = (np.exp(s - z) * v_scale[:, h // G]).max(axis=1, initial=0)
+    spread = np.log2(v_scale.max(initial=1e-30) / v_scale.min(initial=1e30)) if L else 0
+    ds = (D + 8) * 2.0**-24 * sabs + max(0, spread + 16) * 2.0**-24
+    rel = 2 * ds + 2.0**-18 + 2.0**-21 + (2.0**-12 if bf16 else 0)
+    bo = ((2.0**-8 if bf16 else 2.0**-24) * np.abs(ref) + rel[:, :, None] * (absv + np.abs(ref)) +
+          (see.sum(axis=1)[:, None] * (2.0**-23 if bf16 else 2.0**-29) * 448 * top)[:, :, None] + 1e-44)
+    bl = ds.T + 2.0**-19 + 2.0**-22 * np.maximum(np.abs(np.where(np.isfinite(rl), rl, 0)), 1)
+    return ref, rl, bo, bl
+
+
+def check_rows(out, lse, ref, rl, bo, bl, what):
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(l), empty), what
+    assert np.isfinite(o).all() and (o[empty.T] == 0).all(), what
+    worst = [float((np.abs(o - ref) / bo).max()), float((np.abs(np.where(empty, 0, l) - np.where(empty, 0, rl)) / bl).max())]
+    _record(f"{what} out", worst[0], 1.0)
+    _record(f"{what} lse", worst[1], 1.0)
+    assert max(worst) <= 1, (what, worst)
+
+
+ROWS = [(40, BF16), (140, BF16), (300, BF16)]
+
+
+@pytest.mark.parametrize("order", ["small first", "large first"])
+@pytest.mark.parametrize("what", ["keys", "values", "both"])
+@pytest.mark.parametrize("ratio", [2.0**-12, 2.0**-18, 2.0**-33])
+@pytest.mark.parametrize("n,dtype", ROWS)
+def test_rows_that_see_small_blocks_beside_rows_that_see_large_ones(n, dtype, ratio, what, order):
+    """One half of a cache holds keys or values `ratio` times as large as the other's.  Half of the rows see that half
+    alone (their queries as much larger, so that their scores matter); the others see large blocks, or both."""
+    L, D, page, W = 1300, 64, 16, 600
+    half = 656  # whole pages, inside a tile
+    c = Cache([L], 2, D, page)
+    mag = torch.ones(L, 1, 1, device="cuda")
+    small = slice(0, half) if order == "small first" else slice(half, L)
+    mag[small] = ratio
+    k, v = randn(L, 2, D, dtype=F32), randn(L, 2, D, dtype=F32, seed=1)
+    c.append(k * mag if what != "values" else k, v * mag if what != "keys" else v, [L], [0], check=False)
+    early = np.arange(n) % 2 == 0
+    if order == "small first":  # the first rows see small blocks only, the others both
+        pos, window = np.where(early, half - 1 - np.arange(n), L - 1 - np.arange(n)), 0
+    else:  # by the window: rows at the end see small blocks only, the others large ones only
+        pos, window = np.where(early, L - 1 - np.arange(n) % 40, half - 1 - np.arange(n)), W
+    q = randn(n, 4, D, dtype=F32, seed=2)
+    if what != "values":
+        q[torch.from_numpy(early).cuda()] *= 1 / ratio
+    q = q.to(dtype)
+    out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32([L]), i32([0, n]), q_pos=i32(pos), window=window)
+    ref = reference(c, 0, q, L, pos, window)
+    check_rows(out, lse, *ref, what=f"beside {n} {what} {order}")
+    check_ok()
