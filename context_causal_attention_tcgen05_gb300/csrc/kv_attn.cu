@@ -16,10 +16,10 @@
 // brings it) Q^T (B), and O^T [D x rows*parts] = V^T (A, MN-major, the same page bytes)
 // P^T (B, MN-major).  No code is converted or moved by a thread, and the few query rows
 // cost little as the N side.  Thread t owns token t: its key and value scale are one
-// value for all rows, the masks two comparisons a row.  The running maximum is renewed
-// only when a weight times its value scale grows to 2^3 times the largest at the last
-// renewal (a warpgroup's vote), so a usual tile needs no reduction; sums stay per thread
-// to the end.
+// value for all rows, the masks two comparisons a row.  A row's reference m follows its
+// largest product of a weight and a value scale, whatever the scales that other rows see,
+// and is renewed only when one grows to 2^3 times the largest at the last renewal (a
+// warpgroup's vote), so a usual tile needs no reduction; sums stay per thread to the end.
 //
 // Bound by HBM: 2*D bytes a token and head.  The work, every (sequence, row tile, head)
 // unit's tiles of 128 tokens in one line, is cut into equal runs, one a CTA (two CTAs an
@@ -43,11 +43,14 @@ constexpr int kMaxRows = 16;       // largest row tile
 constexpr int kMinRows = 4;        // smallest
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
-// The reference m of a row's weights 2^(x - m) is its largest score less kLog2Unit, renewed when a
-// score passes m + kLog2Range: weights stay under 2^8 (e4m3 ends at 448, and a weight's whole number
-// counts steps of 2^-23).  The last step of three parts is 2^-17, 2^-22 of the largest weight, that of
-// eight 2^-28.
-constexpr float kLog2Unit = 5.0f, kLog2Range = 8.0f;
+// A row's weights are 2^(x - m) times their value scales in units of ev, the largest one seen so far.
+// Its reference m puts the largest of them at 2^kLog2Unit, and is renewed when one passes 2^kLog2Range
+// (e4m3 ends at 448, and a weight's whole number counts steps of 2^-23).  The last step of three parts
+// is 2^-17, 2^-22 of the largest weight, that of eight 2^-28.  Where ev grows, m falls with it, so that
+// a row that sees only small scales keeps its unit: by up to kLog2Fall a unit of work, and a score
+// stays within kLog2Far of m, which keeps the sums under 2^117.
+constexpr float kLog2Unit = 5.0f, kLog2Range = 8.0f, kLog2Far = 60.0f;
+constexpr int kLog2Fall = 40;
 constexpr float kNoMax = -1e30f;  // of a row that has seen nothing: finite, so that -inf less it is -inf
 constexpr float kHidden = -1.0f;    // scale slot of a page that is not loaded
 
@@ -591,6 +594,7 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
           l[r] = 0.f;
         }
         float ev = 0.f, inv_ev = INFINITY;  // largest value scale so far: the weights' unit
+        int fall = kLog2Fall;               // what is left of it
         for (int t = 0; t < n; ++t, ++j) {
           const int key0 = (un.tile0 + t) * BK, key = key0 + gt, st = j % ST, buf = j & 1;
           ok &= wait(&ctl.s_full[buf], j >> 1);
@@ -618,7 +622,7 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
           // logarithm) has to stay under 2^kLog2Range; larger scales alone are no reason to renew
           const float vw = there && key >= un.lo_min && key < un.hi_max && vs > 0.f ? vs : 0.f;
           float fv = vw * (vw > 0.f ? inv_ev : 0.f);
-          const float room = fminf(kLog2Range + 127.f - (float)(__float_as_uint(fv) >> 23), 2 * kLog2Range);
+          const float room = fminf(kLog2Range + 127.f - (float)(__float_as_uint(fv) >> 23), kLog2Far);
           bool grow = fv > 8.f;
 #pragma unroll
           for (int r = 0; r < NR; ++r) grow |= x[r] > m[r] + room;
@@ -628,25 +632,30 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
             auto ordered = [](float f) { const int i = __float_as_int(f); return i ^ ((i >> 31) & 0x7fffffff); };
             auto back = [](int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); };
             int(*red)[NR + 1] = ctl.wred[g][renewals++ & 1];
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              const int top = __reduce_max_sync(0xffffffffu, ordered(x[r] == x[r] ? x[r] : -INFINITY));
-              if (lane == 0) red[wq][r] = top;
-            }
             const int e_top = __reduce_max_sync(0xffffffffu, __float_as_int(vw));
             if (lane == 0) red[wq][NR] = e_top;
             sync_128(g);
             float e = fmaxf(__int_as_float(max(max(red[0][NR], red[1][NR]), max(red[2][NR], red[3][NR]))), ev);
             e = fmaxf(e, 1.17549435e-38f);
             const float ef = ev / e;
+            const int drop = ev > 0.f ? min((__float_as_int(e) >> 23) - (__float_as_int(ev) >> 23), fall) : 0;
+            fall -= drop;
             ev = e;
             inv_ev = 1.f / e;
             fv = vw * inv_ev;
+            // logarithm of the value scale; smaller ones count as 2^(kLog2Unit - kLog2Far)
+            const float lv = fmaxf((float)((int)(__float_as_uint(fv) >> 23) - 127), kLog2Unit - kLog2Far);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const int top = __reduce_max_sync(0xffffffffu, ordered(x[r] == x[r] ? x[r] + lv : -INFINITY));
+              if (lane == 0) red[wq][r] = top;
+            }
+            sync_128(g);
             float alpha[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
               const float mt = back(max(max(red[0][r], red[1][r]), max(red[2][r], red[3][r])));
-              const float mn = fmaxf(m[r], mt - kLog2Unit);
+              const float mn = fmaxf(m[r] - (float)drop, mt - kLog2Unit);
               alpha[r] = ptx::ex2_approx(m[r] - mn);
               l[r] *= alpha[r];
               m[r] = mn;
@@ -747,7 +756,7 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
                 else static_cast<float*>(a.out)[at] = y;
               }
               if (gt == 0)
-                a.lse[(int64_t)h * a.rows + row] = sum == 0.f ? -INFINITY : (m[r] + log2f(sum)) * kLn2;
+                a.lse[(int64_t)h * a.rows + row] = lse_of(m[r], sum);
             }
           }
         }

@@ -973,7 +973,7 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
       }
       if (valid) {
         if (un.part >= 0) ws.ml[un.part * RT + r_unit] = make_float2(m, l);
-        else a.lse[(int64_t)h * a.rows + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        else a.lse[(int64_t)h * a.rows + row] = lse_of(m, l);
       }
       if (halves) {  // nobody writes Q again before every row has been added
         ptx::mbar_arrive(&ctl.half_free);

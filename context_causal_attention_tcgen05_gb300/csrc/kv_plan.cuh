@@ -36,6 +36,13 @@ constexpr int kRowsMaxPairs = 80;  // CTA pairs its workspace has partial result
 constexpr int BK = 128;  // tokens per tile
 constexpr float kLn2 = 0.6931471805599453f;
 
+// log(sum * 2^m), -inf for an empty sum.  m may lie far from the result, with the sum as much larger:
+// the sum's exponent joins it first.
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  const int e = min(max((int)(__float_as_uint(sum) >> 23) - 127, -126), 126);  // (of NaN and infinity: any)
+  return sum == 0.f ? -INFINITY : (m + (float)e + log2f(sum * pow2i(-e))) * kLn2;
+}
+
 // Result record of a (row slot, head) unit for the join.
 struct UnitInfo {
   int32_t row;    // first packed (query row * G + g) of the unit
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const Cac
 #pragma unroll
     for (int e = 0; e < EPL; ++e) static_cast<float*>(a.out)[at + e] = acc[e] * inv;
   }
-  if (lane == 0) a.lse[(int64_t)h * a.rows + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  if (lane == 0) a.lse[(int64_t)h * a.rows + row] = lse_of(mx, sum);
 }
 
 template <int D, int RT, bool kBf16>

@@ -443,9 +443,10 @@ typedef struct {
  *   out = 0 and lse = -inf.  A row that sees any token of a block whose key or value
  *   scale is NaN gets NaN in out and lse.
  * Supported: Hq % Hkv == 0; D in {64, 128}; CP_F32 and CP_BF16.  Scores and sums are
- * fp32; weights are kept relative to a row's largest and to the largest value scale
- * that any row beside it sees, so a row is exact to about 2^-22 (bf16) or 2^-28
- * (fp32) of the product of the two.  workspace >= cp_workspace_size(CP_OP_KV_ATTENTION, rows, Hq, Hkv, D, dtype,
+ * fp32.  A row's weights are kept in steps of 2^-22 (bf16) or 2^-28 (fp32) of its own
+ * largest product of a weight and a value scale, while the value scales that rows of
+ * the call see lie within 2^40 of one another; CP_BF16 also rounds each to 11 bits
+ * (2^-12 of itself).  workspace >= cp_workspace_size(CP_OP_KV_ATTENTION, rows, Hq, Hkv, D, dtype,
  * n_seqs, 0) bytes; calls that may overlap on the GPU need workspaces of their own. */
 CP_API cp_status cp_kv_cache_attention(const cp_kv_cache* cache, const void* q, int64_t rows,
                                        int64_t q_row_stride, int32_t Hq, int32_t dtype, const int32_t* cu_q,

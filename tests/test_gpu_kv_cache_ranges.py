@@ -64,7 +64,7 @@ def check_rows(out, lse, ref, rl, bo, bl, what):
     assert max(worst) <= 1, (what, worst)
 
 
-ROWS = [(40, BF16), (140, BF16), (300, BF16)]
+ROWS = [(2, BF16), (4, BF16), (9, BF16), (40, BF16), (140, BF16), (300, BF16), (1, F32), (3, F32), (20, F32)]
 
 
 @pytest.mark.parametrize("order", ["small first", "large first"])
@@ -94,4 +94,20 @@ def test_rows_that_see_small_blocks_beside_rows_that_see_large_ones(n, dtype, ra
     out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32([L]), i32([0, n]), q_pos=i32(pos), window=window)
     ref = reference(c, 0, q, L, pos, window)
     check_rows(out, lse, *ref, what=f"beside {n} {what} {order}")
+    check_ok()
+
+
+@pytest.mark.parametrize("n,dtype", ROWS)
+def test_large_values_under_small_weights(n, dtype):
+    """A page whose values are 2^16 as large as the rest, under weights about as small: both halves of the sum count."""
+    L, D = 1100, 128
+    c = Cache([L], 1, D, 32)
+    k, v = randn(L, 1, D, dtype=F32) * 0.2, randn(L, 1, D, dtype=F32, seed=1)
+    v[320:352] *= 2.0**16
+    k[320:352] -= 8 * np.log(2) / D**0.5  # q is near 1 in every element: 2 * 8 log 2 lower scores
+    c.append(k, v, [L], [0], check=False)
+    q = (2 + 0.2 * randn(n, 4, D, dtype=F32, seed=2)).to(dtype)
+    out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32([L]), i32([0, n]))
+    ref = reference(c, 0, q, L, np.arange(L - n, L))
+    check_rows(out, lse, *ref, what=f"small weights {n}")
     check_ok()
