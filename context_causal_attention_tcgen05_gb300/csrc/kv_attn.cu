@@ -347,12 +347,13 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
         const SlotSeq& q = sr.q;
         const int r0 = sr.r0, nrows = sr.nrows, t0 = sr.t0(), t1 = sr.t1();
         const Piece pc = unit_piece<C::kCost>(run, f, off, t1 - t0);
-        if (pc.k1 > pc.k0) {
-          const int n = pc.k1 - pc.k0;
-          const int buf = u & 1;
-          if (u >= 2) ok = wait(&ctl.u_empty[buf], (u >> 1) - 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+        const int n = pc.k1 - pc.k0, buf = u & 1;
+        // The join goes by the records, so each of the run's is written, after a wait that gave up too.
+        if (n > 0 && pc.k0 == 0 && lane == 0)
+          ws.info[(int64_t)slot * a.Hkv + head] =
+              unit_record<C::kCost>(run, blockIdx.x, q.c0 * a.G + r0, nrows, f, off, t1 - t0);
+        if (n > 0 && ok && u >= 2) ok = __all_sync(0xffffffffu, wait(&ctl.u_empty[buf], (u >> 1) - 1));
+        if (n > 0 && ok) {
           Unit<RT>& un = ctl.unit[buf];
           if (lane == 0) {
             un.b = q.b;
@@ -379,9 +380,6 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
             un.hi_min = hi_min;
             un.lo_min = sr.lo;
             un.hi_max = sr.hi;
-            if (pc.k0 == 0)
-              ws.info[(int64_t)slot * a.Hkv + head] =
-                  unit_record<C::kCost>(run, blockIdx.x, un.row, nrows, f, off, t1 - t0);
           }
           // q of the unit's rows, split into e4m3 parts.
           // 32/RT lanes a row; rolled loops, as this code too is met cold.

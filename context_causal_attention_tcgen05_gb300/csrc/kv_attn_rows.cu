@@ -462,8 +462,13 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
         const SlotSeq& q = sr.q;
         const int b = q.b, t0 = sr.t0(), t1 = sr.t1();
         const Piece pc = unit_piece<kCost>(run, f, off, t1 - t0);
-        if (pc.k1 > pc.k0) {
-          const int n = pc.k1 - pc.k0, tile0 = t0 + pc.k0;
+        const int n = pc.k1 - pc.k0, tile0 = t0 + pc.k0;
+        // The join goes by the records, so each of the run's is written, after a wait that gave up too.
+        if (n > 0 && pc.k0 == 0 && rank == 0 && lane == 0)
+          ws.info[(int64_t)slot * a.Hkv + head] =
+              unit_record<kCost>(run, pair, q.c0 * a.G + sr.r0, sr.nrows, f, off, t1 - t0);
+        if (n > 0 && ok && u >= 2) ok = __all_sync(0xffffffffu, wait(&ctl.u_empty[u & 1], (u >> 1) - 1));
+        if (n > 0 && ok) {
           const int32_t* table = a.page_table + (int64_t)b * a.max_pages;
           const int p0 = tile0 * ppt, p_end = min((tile0 + n) * ppt, (q.len + a.page - 1) / a.page);
           // the unit's largest scales, among the pages that some row sees: the others' tokens count as zeros
@@ -488,9 +493,6 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
           vr = fmaxf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vr))), 1.17549435e-38f);
           bad = __any_sync(0xffffffffu, bad);
           const bool wide = __any_sync(0xffffffffu, k_min < kr * kKeySpan || v_min < vr * kValueSpan);
-          if (u >= 2) ok = wait(&ctl.u_empty[u & 1], (u >> 1) - 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
           if (lane == 0) {
             Unit& un = ctl.unit[u & 1];
             un.b = b;
@@ -506,9 +508,6 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
             un.special = (bad ? kBad : 0) | (wide ? kWide : 0);
             un.k_ref = wide ? 1.f : kr;
             un.v_ref = vr;
-            if (pc.k0 == 0 && rank == 0)
-              ws.info[(int64_t)slot * a.Hkv + head] =
-                  unit_record<kCost>(run, pair, q.c0 * a.G + sr.r0, sr.nrows, f, off, t1 - t0);
             ptx::mbar_arrive(&ctl.u_full[u & 1]);
           }
           __syncwarp();
@@ -565,8 +564,7 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
             if (lane == 0) ptx::mbar_arrive_expect_tx(&ctl.v8_full[st], v_bytes * __popc(have));
             __syncwarp();
           }
-          if (!ok) break;
-          ++u;
+          if (ok) ++u;
         }
         f += pc.take;
         off = 0;

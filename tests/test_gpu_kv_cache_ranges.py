@@ -7,7 +7,7 @@ import torch
 import context_causal_attention_tcgen05_gb300 as cpa
 from gpu_common import _record, check_ok, need_gpu
 from oracle import serving
-from test_gpu_kv_cache import BF16, F32, Cache, i32, randn
+from test_gpu_kv_cache import BF16, F32, Cache, filled, i32, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,33 @@ def test_large_values_under_small_weights(n, dtype):
     ref = reference(c, 0, q, L, np.arange(L - n, L))
     check_rows(out, lse, *ref, what=f"small weights {n}")
     check_ok()
+
+
+@pytest.mark.parametrize("n,dtype,tile", [(1, BF16, 4), (2, BF16, 8), (4, BF16, 16), (70, BF16, 512), (1, F32, 4), (6, F32, 8)])
+def test_every_unit_has_its_record(n, dtype, tile):
+    """The second launch takes rows and partial results by the records that the first leaves in the workspace, which may
+    hold anything before: every row of every head is in one record, and none leads outside the batch or the partial
+    results (512 workers' at most)."""
+    lens, news = [3000, 0, 40, 700, 2], [n, 2, n, 0, 1]
+    c = filled(lens, 2, 128, 32, dtype)
+    rows, G = sum(news), 4
+    q = randn(rows, 2 * G, 128, dtype=dtype, seed=6)
+    ws = torch.full((cpa.cp_workspace_size("kv_attention", rows, 2 * G, 2, 128, cpa._dt(q), len(lens)),), 0x7F,
+                    dtype=torch.uint8, device="cuda")
+    cu = np.concatenate([[0], np.cumsum(news)])
+    out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32(lens), i32(cu), window=2500, workspace=ws)
+    check_ok()
+    for b, (m, L) in enumerate(zip(news, lens)):
+        r = slice(cu[b], cu[b + 1])
+        if m:
+            check_rows(out[r], lse[:, r], *reference(c, b, q[r], L, np.arange(L - m, L), 2500), what=f"records {n}")
+    slots = rows * G // tile + len(lens)
+    records = ws[:slots * 2 * 16].cpu().numpy().view(np.int32).reshape(slots, 2, 4)
+    for h in range(2):
+        seen = np.zeros(rows * G, int)
+        for row, nrows, c0, c1 in records[:, h].tolist():
+            assert 0 <= nrows <= tile
+            if nrows:
+                assert 0 <= row and row + nrows <= rows * G and (c0 == -1 or 0 <= c0 <= c1 < 512)
+                seen[row:row + nrows] += 1
+        assert (seen == 1).all()
