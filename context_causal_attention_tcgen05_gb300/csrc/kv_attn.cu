@@ -52,7 +52,7 @@ constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kLog2Unit = 5.0f, kLog2Range = 8.0f, kLog2Far = 60.0f;
 constexpr int kLog2Fall = 40;
 constexpr float kNoMax = -1e30f;  // of a row that has seen nothing: finite, so that -inf less it is -inf
-constexpr float kHidden = -1.0f;    // scale slot of a page that is not loaded
+constexpr float kHidden = -1.0f;    // scale slot of a page that is not brought
 
 // Row tile RT, parts of q and of a weight, softmax warpgroups.
 template <int D_, int RT_, int NPQ_, int NPP_, int NG_>
@@ -361,6 +361,8 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
             un.tile0 = t0 + pc.k0;
             un.ntiles = n;
             un.len = q.len;
+            un.lo_min = sr.lo;
+            un.hi_max = sr.hi;
             un.nrows = nrows;
             un.row = q.c0 * a.G + r0;
             un.part = n == t1 - t0 ? -1 : 2 * (int)blockIdx.x + (pc.k0 > 0 ? 0 : 1);
@@ -378,8 +380,6 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
           if (lane == 0) {
             un.lo_max = lo_max;
             un.hi_min = hi_min;
-            un.lo_min = sr.lo;
-            un.hi_max = sr.hi;
           }
           // q of the unit's rows, split into e4m3 parts.
           // 32/RT lanes a row; rolled loops, as this code too is met cold.
@@ -454,7 +454,10 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
         if (n == 0) break;
         const int hk = un.hk;
         const int32_t* table = a.page_table + (int64_t)un.b * a.max_pages;
-        const int p0 = un.tile0 * ppt, p_end = min((un.tile0 + n) * ppt, (un.len + a.page - 1) / a.page);
+        // pages [p_first, p_end) of its tiles hold tokens that some row sees; the others are not brought and
+        // need not exist (those before a window may have been given back)
+        const int p0 = un.tile0 * ppt, p_first = un.lo_min / a.page;
+        const int p_end = min((un.tile0 + n) * ppt, (un.hi_max + a.page - 1) / a.page);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&ctl.u_empty[u & 1]);
         // 32 pages at a time, their ids and scales one batch ahead
@@ -463,7 +466,7 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
         auto fetch = [&](int p, int& i, float& k, float& v) {
           i = -1;
           k = v = kHidden;
-          if (p + lane < p_end) {
+          if (p + lane >= p_first && p + lane < p_end) {
             i = __ldg(table + p + lane);
             if (i < 0 || i >= a.n_pages) {
               record_device_error(a.err, kDevIndex);
@@ -709,7 +712,7 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
                   make_uint4(n0 & kEven, (n0 >> 4) & kEven, n1 & kEven, (n1 >> 4) & kEven);
             }
           }
-          if (!there && g == 0) {  // a token past the end or of no page: its bytes may be anything
+          if (!there && g == 0) {  // a token past the end or of a page that was not brought: its bytes may be anything
             (void)wait(&ctl.kv_full[st], j / ST);
             uint4* vz = reinterpret_cast<uint4*>(smem + C::kV + st * C::kTile + gt * D);
 #pragma unroll

@@ -470,18 +470,19 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
         if (n > 0 && ok && u >= 2) ok = __all_sync(0xffffffffu, wait(&ctl.u_empty[u & 1], (u >> 1) - 1));
         if (n > 0 && ok) {
           const int32_t* table = a.page_table + (int64_t)b * a.max_pages;
-          const int p0 = tile0 * ppt, p_end = min((tile0 + n) * ppt, (q.len + a.page - 1) / a.page);
-          // the unit's largest scales, among the pages that some row sees: the others' tokens count as zeros
-          const int seen0 = sr.lo / a.page, seen1 = (sr.hi + a.page - 1) / a.page;
+          // pages [p_first, p_end) of its tiles hold tokens that some row sees; the others' tokens count as
+          // zeros and need not exist (those before a window may have been given back)
+          const int p0 = tile0 * ppt, p_first = max(p0, sr.lo / a.page);
+          const int p_end = min((tile0 + n) * ppt, (sr.hi + a.page - 1) / a.page);
           float kr = 0.f, vr = 0.f, k_min = INFINITY, v_min = INFINITY;
           bool bad = false;
 #pragma unroll 4
-          for (int p = p0 + lane; p < p_end; p += 32) {
+          for (int p = p_first + lane; p < p_end; p += 32) {
             const int id = __ldg(table + p);
             if (id < 0 || id >= a.n_pages) {
               record_device_error(a.err, kDevIndex);
               bad = true;
-            } else if (p >= seen0 && p < seen1) {
+            } else {
               const float k = __ldg(a.k_scale + (int64_t)id * a.Hkv + head), v = __ldg(a.v_scale + (int64_t)id * a.Hkv + head);
               kr = fmaxf(kr, k);  // (NaN is none of these)
               vr = fmaxf(vr, v);
@@ -518,11 +519,11 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
           auto fetch = [&](int p, int& i, uint32_t& k2, uint32_t& v2) {
             i = -1;
             k2 = v2 = 0u;
-            if (p + lane < p_end) {
+            if (p + lane >= p_first && p + lane < p_end) {
               i = __ldg(table + p + lane);
               if (i < 0 || i >= a.n_pages) {
                 i = -1;
-              } else if (p + lane >= seen0 && p + lane < seen1) {
+              } else {
                 const float k = __ldg(a.k_scale + (int64_t)i * a.Hkv + head), v = __ldg(a.v_scale + (int64_t)i * a.Hkv + head);
                 const float kf = fmaf(k, k_inv, one), vf = fmaf(v, v_inv, one);
                 k2 = v != v ? 0x7e007e00u : pack_f16x2(kf, kf);  // a NaN scale reaches the scores

@@ -373,7 +373,9 @@ CP_API cp_status cp_ulysses_attention_bwd(const void* q, const void* k, const vo
  * e4m3 keeps 4 significant bits at any scale, so a power of two costs no precision
  * inside its range and makes every product with a scale exact.
  *   page_table [n_seqs, max_pages] (device): page_table[b][t / page] is the page of
- *   token t of sequence b.  Entries past a sequence's tokens are not read.  Pages may
+ *   token t of sequence b.  Entries past a sequence's tokens are not read, nor those of
+ *   pages that no row of an attention call sees (all before its window: such a page may
+ *   be given back, its entry set to -1).  Pages may
  *   be shared between sequences for reading (common prefixes); a page that
  *   cp_kv_cache_append writes belongs to one sequence.
  * page in {16, 32, 64, 128}, D in {64, 128} (CP_ERR_SHAPE).  All arrays are the

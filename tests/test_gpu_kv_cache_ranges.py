@@ -141,3 +141,31 @@ def test_every_unit_has_its_record(n, dtype, tile):
                 assert 0 <= row and row + nrows <= rows * G and (c0 == -1 or 0 <= c0 <= c1 < 512)
                 seen[row:row + nrows] += 1
         assert (seen == 1).all()
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("n,dtype", [(1, BF16), (5, F32), (70, BF16), (300, BF16)])
+def test_pages_that_no_row_sees_need_not_exist(n, dtype, page):
+    """Pages before every row's window and behind every row's position may have been given back: their entries are not
+    used."""
+    L, W, last = 2000, 130, 1500  # the last row's position
+    c = filled([L], 2, 128, page, dtype)
+    pos = last - n + 1 + np.arange(n)
+    lo, hi = (pos[0] - W + 1) // page, last // page + 1
+    c.t[4][0, :lo] = -1
+    c.t[4][0, hi:] = 10**6
+    q = randn(n, 8, 128, dtype=dtype, seed=3)
+    out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32([L]), i32([0, n]), window=W, q_pos=i32(pos))
+    check_ok()
+    ref = reference(c, 0, q, L, pos, W)
+    check_rows(out, lse, *ref, what=f"given back {n} {page}")
+    # the window alone: the rows are the last tokens
+    c = filled([L], 2, 128, page, dtype)
+    c.t[4][0, :(L - n - W + 1) // page] = -1
+    out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32([L]), i32([0, n]), window=W)
+    check_ok()
+    check_rows(out, lse, *reference(c, 0, q, L, np.arange(L - n, L), W), what=f"given back by window {n} {page}")
+    # a page that a row sees is still reported
+    c.t[4][0, L // page - 1] = -1
+    cpa.cp_kv_cache_attention(q, *c.args(), i32([L]), i32([0, n]), window=W)
+    assert cpa.cp_check_device_status() == -9
