@@ -260,7 +260,7 @@ __device__ __forceinline__ float join_parts(const uint32_t (&o)[N], int r) {
 template <bool kBf16>
 __device__ __forceinline__ void load8(float (&x)[8], const char* p, int at) {
   if constexpr (kBf16) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p + at * 2));
+    const uint4 w = ld(reinterpret_cast<const uint4*>(p + at * 2));
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -270,7 +270,7 @@ __device__ __forceinline__ void load8(float (&x)[8], const char* p, int at) {
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(p + at * 4) + i);
+      const float4 w = ld(reinterpret_cast<const float4*>(p + at * 4) + i);
       x[4 * i] = w.x;
       x[4 * i + 1] = w.y;
       x[4 * i + 2] = w.z;
@@ -467,13 +467,13 @@ kv_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ 
           i = -1;
           k = v = kHidden;
           if (p + lane >= p_first && p + lane < p_end) {
-            i = __ldg(table + p + lane);
+            i = ld(table + p + lane);
             if (i < 0 || i >= a.n_pages) {
               record_device_error(a.err, kDevIndex);
               i = -1;
             } else {
-              k = __ldg(a.k_scale + (int64_t)i * a.Hkv + hk);
-              v = __ldg(a.v_scale + (int64_t)i * a.Hkv + hk);
+              k = ld(a.k_scale + (int64_t)i * a.Hkv + hk);
+              v = ld(a.v_scale + (int64_t)i * a.Hkv + hk);
             }
           }
         };

@@ -295,7 +295,7 @@ __device__ __forceinline__ void hide(uint32_t (&s)[32], int ch, int ilo, int ihi
   for (int i = 0; i < 32; i += 16) {  // pages are multiples of 16 tokens
     const int key = key0 + ch * 32 + i;
     if (key >= un.len) break;
-    const int id = __ldg(a.page_table + (int64_t)un.b * a.max_pages + key / a.page);
+    const int id = ld(a.page_table + (int64_t)un.b * a.max_pages + key / a.page);
     if (id >= 0 && id < a.n_pages) continue;
 #pragma unroll
     for (int k = 0; k < 16; ++k) s[i + k] = kInf;
@@ -317,10 +317,10 @@ __device__ __forceinline__ float2 wide_tile(const Unit& un, const CacheAttnArgs&
   auto scales = [&](int col) {
     const int key = key0 + col;
     if (key >= un.len) return make_float2(0.f, 0.f);
-    const int id = __ldg(a.page_table + (int64_t)un.b * a.max_pages + key / a.page);
+    const int id = ld(a.page_table + (int64_t)un.b * a.max_pages + key / a.page);
     if (id < 0 || id >= a.n_pages) return make_float2(0.f, 0.f);
     const int64_t at = (int64_t)id * a.Hkv + un.hk;
-    const float f = __ldg(a.k_scale + at) * qs, v = __ldg(a.v_scale + at);
+    const float f = ld(a.k_scale + at) * qs, v = ld(a.v_scale + at);
     // (a score of 0 stays 0 where the factor alone passes fp32)
     return make_float2(f > 3e38f ? 3e38f : f, v > 0.f ? fminf(v * v_inv, 1.f) : 0.f);
   };
@@ -478,12 +478,12 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
           bool bad = false;
 #pragma unroll 4
           for (int p = p_first + lane; p < p_end; p += 32) {
-            const int id = __ldg(table + p);
+            const int id = ld(table + p);
             if (id < 0 || id >= a.n_pages) {
               record_device_error(a.err, kDevIndex);
               bad = true;
             } else {
-              const float k = __ldg(a.k_scale + (int64_t)id * a.Hkv + head), v = __ldg(a.v_scale + (int64_t)id * a.Hkv + head);
+              const float k = ld(a.k_scale + (int64_t)id * a.Hkv + head), v = ld(a.v_scale + (int64_t)id * a.Hkv + head);
               kr = fmaxf(kr, k);  // (NaN is none of these)
               vr = fmaxf(vr, v);
               k_min = fminf(k_min, k);
@@ -520,11 +520,11 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
             i = -1;
             k2 = v2 = 0u;
             if (p + lane >= p_first && p + lane < p_end) {
-              i = __ldg(table + p + lane);
+              i = ld(table + p + lane);
               if (i < 0 || i >= a.n_pages) {
                 i = -1;
               } else {
-                const float k = __ldg(a.k_scale + (int64_t)i * a.Hkv + head), v = __ldg(a.v_scale + (int64_t)i * a.Hkv + head);
+                const float k = ld(a.k_scale + (int64_t)i * a.Hkv + head), v = ld(a.v_scale + (int64_t)i * a.Hkv + head);
                 const float kf = fmaf(k, k_inv, one), vf = fmaf(v, v_inv, one);
                 k2 = v != v ? 0x7e007e00u : pack_f16x2(kf, kf);  // a NaN scale reaches the scores
                 v2 = v != v ? 0u : pack_f16x2(vf, vf);
@@ -756,7 +756,7 @@ kv_attn_rows_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_consta
           const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                             (int64_t)(un.c0 + tok) * a.q_ld + (int64_t)h * D);
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) x[i] = __ldg(src + i);
+          for (int i = 0; i < D / 8; ++i) x[i] = ld(src + i);
         } else {
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const CacheRo
     const int lane = threadIdx.x & 31, i = min(lane, a.n_seqs - 1);
     int first, count;
     seq_rows(a.cu_rows, i, a.rows, &first, &count);
-    const int start = __ldg(a.start + i);
+    const int start = ld(a.start + i);
     const bool le = lane < a.n_seqs && first / page + 2 * lane <= slot;
     b = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
     c0 = __shfl_sync(0xffffffffu, first, b);
@@ -71,10 +71,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const CacheRo
     s0 = __shfl_sync(0xffffffffu, start, b);
   } else {
     b = warp_find(a.n_seqs, slot, [&](int i) {
-      return (min(max((int64_t)__ldg(a.cu_rows + i), (int64_t)0), a.rows) / page) + 2 * i;
+      return (min(max((int64_t)ld(a.cu_rows + i), (int64_t)0), a.rows) / page) + 2 * i;
     });
     seq_rows(a.cu_rows, b, a.rows, &c0, &n);
-    s0 = __ldg(a.start + b);
+    s0 = ld(a.start + b);
   }
   if (n == 0) return;
   if (s0 < 0) {
@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const CacheRowsAr
     int lo = 0, hi = a.n_seqs - 1;
     while (lo < hi) {  // largest b with cu_rows[b] <= row
       const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.cu_rows + mid) <= row) lo = mid; else hi = mid - 1;
+      if (ld(a.cu_rows + mid) <= row) lo = mid; else hi = mid - 1;
     }
-    if (row < __ldg(a.cu_rows + lo) || row >= __ldg(a.cu_rows + lo + 1)) {  // no sequence's row: left as it is
+    if (row < ld(a.cu_rows + lo) || row >= ld(a.cu_rows + lo + 1)) {  // no sequence's row: left as it is
       blk0[i] = kNoRow;
       continue;
     }
-    const int64_t tok = (int64_t)__ldg(a.start + lo) + row - __ldg(a.cu_rows + lo);
+    const int64_t tok = (int64_t)ld(a.start + lo) + row - ld(a.cu_rows + lo);
     int id = -1;
     if (tok < 0) record_device_error(a.err, kDevIndex);
     else id = page_id(a.page_table, a.max_pages, a.n_pages, lo, tok / a.page, a.err);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const CacheRowsAr
     if (blk0[i] >= 0) {
       const int64_t blk = blk0[i] + head;
       const uint2 w = __ldcs(reinterpret_cast<const uint2*>(codes + (blk * a.page + at[i]) * a.D + c));
-      const float s = __ldg(scales + blk);
+      const float s = ld(scales + blk);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t u = k ? w.y : w.x;

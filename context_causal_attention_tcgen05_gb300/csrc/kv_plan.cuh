@@ -93,7 +93,7 @@ __device__ __forceinline__ void row_bounds(const CacheAttnArgs& a, const SlotSeq
   lo = 0;
   hi = s.len;
   if (!a.causal) return;
-  const int64_t d = a.q_pos ? (int64_t)__ldg(a.q_pos + s.c0 + i) - a.k_offset
+  const int64_t d = a.q_pos ? (int64_t)ld(a.q_pos + s.c0 + i) - a.k_offset
                             : ((int64_t)s.len - s.n + i) * a.k_stride;
   const int2 r = row_bounds_at(d, a.k_stride, a.window, s.len);
   lo = r.x;
@@ -200,8 +200,8 @@ __device__ __forceinline__ Run plan_run(const CacheAttnArgs& a, const WsPtrs& ws
   const bool staged = a.n_seqs <= cap_seqs;
   bool bad = false;
   for (int i = tid; i <= a.n_seqs; i += kThreads) {
-    const int first = __ldg(a.cu_q + i), next = __ldg(a.cu_q + min(i + 1, a.n_seqs));
-    const int len = __ldg(a.kv_len + min(i, a.n_seqs - 1));
+    const int first = ld(a.cu_q + i), next = ld(a.cu_q + min(i + 1, a.n_seqs));
+    const int len = ld(a.kv_len + min(i, a.n_seqs - 1));
     bad |= next < first;
     if (staged) {
       lens[i] = first;

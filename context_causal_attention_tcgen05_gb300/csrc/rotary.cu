@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
           const int r = t / pairs, i = t - r * pairs;
           int ax = 0;
           while (ax + 1 < a.n_axes && i >= a.axis_end[ax]) ++ax;
-          const int64_t pos = __ldg(a.positions + (int64_t)ax * a.S + s0 + r);
-          const float f = __ldg(a.inv_freq + i);
+          const int64_t pos = ld(a.positions + (int64_t)ax * a.S + s0 + r);
+          const float f = ld(a.inv_freq + i);
           const uint64_t prod = turn_fraction(f) * (uint64_t)pos;              // whole turns drop out
           float frac = (float)(int32_t)(prod >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
           if (!isfinite(f)) frac = __int_as_float(0x7fc00000);

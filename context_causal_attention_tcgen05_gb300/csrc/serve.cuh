@@ -17,6 +17,13 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// Memory that a kernel before may still be writing after this one has started is read by ordinary loads:
+// the read-only path is for what nothing writes while the kernel lives, and the compiler may move such a
+// load in front of the wait.
+template <class T>
+__device__ __forceinline__ T ld(const T* p) {
+  return *p;
+}
 template <class... P, class... A>
 cp_status launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const char* what,
                          const A&... args) {
@@ -153,8 +160,8 @@ __device__ __forceinline__ int warp_find(int n, int64_t x, F f) {
 
 // First and number of packed rows of sequence b, clamped into [0, rows].
 __device__ __forceinline__ void seq_rows(const int32_t* cu, int b, int64_t rows, int* first, int* n) {
-  const int64_t r0 = min(max((int64_t)__ldg(cu + b), (int64_t)0), rows);
-  const int64_t r1 = min(max((int64_t)__ldg(cu + b + 1), r0), rows);
+  const int64_t r0 = min(max((int64_t)ld(cu + b), (int64_t)0), rows);
+  const int64_t r1 = min(max((int64_t)ld(cu + b + 1), r0), rows);
   *first = (int)r0;
   *n = (int)(r1 - r0);
 }
@@ -164,7 +171,7 @@ __device__ __forceinline__ void seq_rows(const int32_t* cu, int b, int64_t rows,
 __device__ __forceinline__ int page_id(const int32_t* table, int max_pages, int n_pages, int b, int64_t p,
                                        int32_t* err) {
   int id = -1;
-  if (p >= 0 && p < max_pages) id = __ldg(table + (int64_t)b * max_pages + p);
+  if (p >= 0 && p < max_pages) id = ld(table + (int64_t)b * max_pages + p);
   if (id < 0 || id >= n_pages) {
     record_device_error(err, kDevIndex);
     return -1;
