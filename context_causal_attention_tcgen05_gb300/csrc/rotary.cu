@@ -4,8 +4,10 @@
 // matter, so the angle is kept as a 64-bit fixed-point fraction of a turn: with
 // F = inv_freq / (2 pi) * 2^64, position * F modulo 2^64 drops the whole turns by
 // itself, at any position.  F is formed from the 24 bits of inv_freq and 64 bits of
-// 1 / (2 pi) in integers, so it is off by about one unit and the angle of a 32-bit
-// position by 2^-32 of a turn.
+// 1 / (2 pi) in integers, so it is off by at most two units and the angle of a 32-bit
+// position by 2^-32 of a turn.  Quarter turns are taken off in integers, so what is rounded
+// to fp32 is at most an eighth of a turn, and cos and sin are right to their own size (fp32
+// results are off by 3.9e-8 of theirs in the 2-norm: a rounding each of cos, sin, a product, a sum).
 #include "serve.cuh"
 
 namespace cpa {
@@ -37,7 +39,7 @@ struct Place {
 // Bound by HBM: every element is read and written once.  A block takes a few rows; cos and sin of
 // each of their pairs are computed once for all heads, while the first loads are on their way.
 // 64 bytes a thread are loaded before any are written (q and k of 65536 rows, 40 heads of 128, bf16:
-// 206 us, 6.5 TB/s; half of 64 heads of 8192 fp32 rows: 84 us, 6.3 TB/s, against 107 with 16 bytes;
+// 207 us, 6.5 TB/s; half of 64 heads of 8192 fp32 rows: 85 us, 6.3 TB/s, against 107 with 16 bytes;
 // 128 bytes, which leave fewer blocks a SM, 93).
 template <bool kBf16, bool kInter>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, int rows_per_block) {
@@ -99,11 +101,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
           while (ax + 1 < a.n_axes && i >= a.axis_end[ax]) ++ax;
           const int64_t pos = ld(a.positions + (int64_t)ax * a.S + s0 + r);
           const float f = ld(a.inv_freq + i);
-          const uint64_t prod = turn_fraction(f) * (uint64_t)pos;              // whole turns drop out
-          float frac = (float)(int32_t)(prod >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
-          if (!isfinite(f)) frac = __int_as_float(0x7fc00000);
+          const uint64_t turn = turn_fraction(f) * (uint64_t)pos;  // whole turns drop out
+          const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
+          float rest = (float)(int64_t)(turn - ((uint64_t)quarter << 62)) * 0x1p-63f;  // half turns
+          if (!isfinite(f)) rest = __int_as_float(0x7fc00000);
           float sn, c;
-          sincospif(frac, &sn, &c);
+          sincospif(rest, &sn, &c);
+          const float c4 = quarter & 1 ? -sn : c, s4 = quarter & 1 ? c : sn;
+          c = quarter & 2 ? -c4 : c4;
+          sn = quarter & 2 ? -s4 : s4;
           cs[t] = make_float2(c, a.inverse ? -sn : sn);
         }
         __syncthreads();
