@@ -169,3 +169,72 @@ def test_pages_that_no_row_sees_need_not_exist(n, dtype, page):
     c.t[4][0, L // page - 1] = -1
     cpa.cp_kv_cache_attention(q, *c.args(), i32([L]), i32([0, n]), window=W)
     assert cpa.cp_check_device_status() == -9
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("singles,chunk", [(20, 200), (90, 200), (3, 40)])
+def test_single_tokens_beside_a_chunk(singles, chunk, dtype):
+    """A ragged batch of single tokens and one prompt's chunk, by either kernel."""
+    rng = np.random.default_rng(5)
+    lens = rng.integers(1, 900, size=singles + 1).tolist()
+    news = [1] * (singles + 1)
+    lens[singles // 2], news[singles // 2] = 1000, chunk
+    c = filled(lens, 2, 128, 64, dtype)
+    q = randn(sum(news), 8, 128, dtype=dtype, seed=5)
+    cu = np.concatenate([[0], np.cumsum(news)])
+    out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32(lens), i32(cu))
+    for b, (n, L) in enumerate(zip(news, lens)):
+        r = slice(cu[b], cu[b + 1])
+        check_rows(out[r], lse[:, r], *reference(c, b, q[r], L, np.arange(L - n, L)), what=f"beside a chunk {singles}")
+    check_ok()
+
+
+@pytest.mark.parametrize("new,dtype", [(1, F32), (30, F32), (1, BF16), (100, BF16)])
+def test_striped_ranks_merge_to_the_whole_they_hold(new, dtype):
+    """Each of P ranks caches its striped tokens; their attentions merge into that of the values the ranks hold."""
+    P, L, H, Hkv, D = 4, 501, 8, 2, 128
+    k, v = randn(L, Hkv, D, dtype=F32), randn(L, Hkv, D, dtype=F32, seed=1)
+    q = randn(new, H, D, dtype=dtype, seed=4)
+    held = [np.zeros((L, Hkv, D)) for _ in range(2)]
+    scale = np.zeros((L, Hkv))
+    o = l = None
+    for r in range(P):
+        n = len(range(r, L, P))
+        part = Cache([n], Hkv, D, 32, seed=r)
+        part.append(k[r::P].contiguous(), v[r::P].contiguous(), [n], [0], check=False)
+        for i in range(2):
+            held[i][r::P] = part.values(i, 0, n)
+        scale[r::P] = part.scales[1][[int(part.table[0][t // 32]) for t in range(n)]]
+        oo, ll = cpa.cp_kv_cache_attention(q, *part.args(), i32([n]), i32([0, new]), q_pos=i32(np.arange(L - new, L)),
+                                           k_offset=r, k_stride=P)
+        oo = oo.float()
+        o, l = (oo, ll) if o is None else cpa.cp_lse_merge(o, l, oo, ll)
+    ref, rl, bo, bl = reference(None, 0, q, L, np.arange(L - new, L), pos_k=np.arange(L), k=held[0], v=held[1], v_scale=scale)
+    _, _, absv, _ = serving.cache_attention(q.double().cpu().numpy(), *held, np.arange(L - new, L), np.arange(L))
+    # each part's result is rounded by itself (its magnitude, weighted, is within absv), its share by its lse's rounding;
+    # a merge takes two exponentials, a logarithm, two products, a sum and a quotient
+    part = (2.0**-8 if dtype == BF16 else 2.0**-24) * absv
+    share = 2 * (bl.T[:, :, None] + 3 * 8 * 2.0**-23) * (absv + np.abs(ref))
+    check_rows(o, l, ref, rl, bo + part + share, bl + 3 * 2.0**-21 * np.maximum(1, np.abs(rl)), what=f"striped merge {new}")
+    check_ok()
+
+
+@pytest.mark.parametrize("n,dtype", [(1, BF16), (3, BF16), (16, BF16), (100, BF16), (300, BF16), (1, F32), (2, F32), (40, F32), (150, F32)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_errors_in_the_2_norm(n, dtype, D):
+    """fp32: scores to a few fp32 roundings, weights to 2^-28, so well under 2^-20 of the result (a weight of 13 bits gives
+    2^-13).  bf16: the result's rounding, up to 2^-8 of its binade's start and so 2^-8 / sqrt 3 of it in the mean, .736 of
+    that for values spread evenly over the binade; weights rounded to 11 bits add under a tenth."""
+    lens = [2000, 700]
+    c = filled(lens, 2, D, 32, dtype, seed=3)
+    q = randn(2 * n, 4, D, dtype=dtype, seed=7)
+    out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32(lens), i32([0, n, 2 * n]))
+    bound = 2.0**-20 if dtype == F32 else 1.1 * 0.736 * 2.0**-8 / 3**0.5
+    for b in range(2):
+        rows = slice(b * n, (b + 1) * n)
+        ref, rl, _, _ = reference(c, b, q[rows], lens[b], np.arange(lens[b] - n, lens[b]))
+        e = np.linalg.norm(out[rows].double().cpu().numpy() - ref) / np.linalg.norm(ref)
+        _record(f"2-norm {n} D={D}", e, bound)
+        assert e <= bound
+        assert np.abs(lse[:, rows].double().cpu().numpy() - rl).max() <= 2.0**-17 * max(1, np.abs(rl).max())
+    check_ok()
