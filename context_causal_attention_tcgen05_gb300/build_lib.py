@@ -5,9 +5,10 @@ file under _build/, then linked into the package directory.  Run as
 ``python -m context_causal_attention_tcgen05_gb300.build_lib``.
 
 ``--debug`` (``build(debug=True)``) builds libcp_attn_debug.so instead, with
--DCP_DEBUG: every kernel checks the indices it computes against its buffers'
-extents, skips an access that fails and records the failure, which
-cp_check_device_status reports as CP_ERR_DEVICE_INDEX.  Load it by setting
+-DCP_DEBUG: every attention, merge and mover kernel checks the indices it
+computes against its buffers' extents, skips an access that fails and records
+the failure, which cp_check_device_status reports as CP_ERR_DEVICE_INDEX (the
+key/value cache kernels check page ids and lengths in every build).  Load it by setting
 CP_ATTN_LIBRARY to its path before the binding loads the library.
 """
 from __future__ import annotations

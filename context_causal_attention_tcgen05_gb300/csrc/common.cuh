@@ -132,7 +132,7 @@ struct BwdArgs {
 enum DeviceError : int32_t {
   kDevOk = 0,
   kDevTimeout = 1,
-  kDevIndex = 2,  // debug builds: an index check failed (the access was skipped)
+  kDevIndex = 2,  // an index check failed (the access was skipped): the cache kernels', or a debug build's
 };
 
 // ---------------------------------------------------------------- host side helpers (api.cu)

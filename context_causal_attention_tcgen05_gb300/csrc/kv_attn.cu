@@ -6,10 +6,12 @@
 // two per (page, head), so the codes go to the tensor cores as they are and the scales
 // are applied to scores and weights.  tcgen05's kind::f8f6f4 multiplies e4m3 exactly
 // and adds in fp32 (measured: 1e-8 relative, as an fp32 chain), so the other operand
-// is split into e4m3 parts without loss: q = 2^e sum_i q_i 16^-i with q_i the e4m3
+// is split into e4m3 parts: q = 2^e sum_i q_i 16^-i with q_i the e4m3
 // rounding of 16 times what the parts before it left, 2 parts for the 8 bits of bf16,
-// 6 for the 24 of fp32.  The weights of bf16 likewise, 3 parts of an 11-bit rounding (fp16);
-// those of fp32 as 32-bit whole numbers in 8 parts of 4 bits: code k < 16 is k 2^-9 (subnormals
+// 6 for the 24 of fp32 (whole for elements down to 2^-13 of the row's largest; smaller ones
+// are off by up to 2^-21 and 2^-37 of it).  The weights of bf16 likewise, 3 parts of an 11-bit
+// rounding (fp16: 2^-12 of each, an eighth of half a step of a bf16 result; their sum is
+// kept whole); those of fp32 as 32-bit whole numbers in 8 parts of 4 bits: code k < 16 is k 2^-9 (subnormals
 // and the first binade are one line), so a digit is its own code and no conversion is needed.
 //
 // Layout.  Keys are the M side: S^T [128 tokens x rows*parts] = K (A, K-major, as TMA
@@ -27,7 +29,7 @@
 // workspace and kv_attn_join_kernel adds them in order, so results do not vary.
 //
 // Roles of a CTA: one or two warpgroups softmax and epilogue (two share the 8 rows of an fp32
-// tile: 24 sequences of 1000 to 4000 tokens, 16 rows, D = 128, in 56.2 us against 57.5), then a
+// tile: 24 sequences of 1000 to 4000 tokens, 16 rows, D = 128, in 56.0 us; 57.5 with one), then a
 // warp each: TMA producer (page ids and scales a batch ahead), MMA issuer (S of tile j+1 before
 // PV of tile j), planner (decodes the next unit, splits its q); of 8 warps the last only helps
 // to plan.
@@ -845,8 +847,9 @@ cp_status make_codes_map(CUtensorMap* m, const void* base, int64_t rows, int D, 
 namespace {
 
 // Many rows a key: the rows kernel.  Its tile costs the same for 1 to 256 rows, this kernel's
-// grows by 16 rows (16 sequences of 8192 tokens, 8 heads of 128: 157 to 163 us against 67 for 16
-// rows, 124 for 32, 176 for 48, 226 for 64; D = 64: 133 to 138 us against 54, 87, 126 and 156).
+// grows by 16 rows (16 sequences of 8192 tokens, 8 heads of 128: 156 to 161 us for 16 to 64 rows
+// against 67 for 16, 123 for 32, 176 for 48, 224 for 64; D = 64: 135 to 141 us against 55, 89, 129 and
+// 159).
 bool many_rows(int64_t rows, int64_t G, int64_t n_seqs, bool is_bf16) { return is_bf16 && rows * G > 32 * n_seqs; }
 
 }  // namespace

@@ -5,7 +5,8 @@
 // query head, so the queries are the M side and the products run in kind::f16: an e4m3
 // code times a power of two down to 2^-15 is exact in fp16, so a page's scale relative to the
 // unit's largest goes into its converted codes; q is scaled to [128, 256) a row (its 8 bits are
-// exact down to 2^-25 of the row's largest), and the weights keep 11 bits.  Codes are converted
+// exact down to 2^-24 of the row's largest), and the weights keep 11 bits (2^-12 of each, an eighth of
+// half a step of a bf16 result; their sum is kept whole).  Codes are converted
 // once per key tile and used by 256 rows.
 // A unit whose seen pages differ by more than kKeySpan or kValueSpan (`wide`) is rare and
 // would lose its small pages so: there the codes are converted as they are and the softmax
@@ -14,7 +15,7 @@
 // Two CTAs on neighbouring SMs work as a pair (cta_group::2): a product has 256 rows, 128 in
 // each CTA, and each CTA holds half of its B operand (64 of the tile's keys for S, half of the
 // head's columns for O).  So a code is converted once for 512 query rows, and an SM reads and
-// converts half a tile.  A chunk of 2048 rows over 32768 tokens, 32 heads: 0.831 ms, 1281 TFLOP/s
+// converts half a tile.  A chunk of 2048 rows over 32768 tokens, 32 heads: 0.828 ms, 1286 TFLOP/s
 // (one CTA a tile, with twice the conversion on each SM: 1.16 ms).
 //
 // One CTA an SM, 16 warps:
@@ -30,7 +31,7 @@
 // A unit of at most 256 rows has one query tile in each CTA; then the two warpgroups take its even
 // and its odd key tiles (order O_w += P_w V_t | S_w = Q K_{t+2}, w = t mod 2), each with sums and an
 // O of its own, and the second's go to the first through shared memory at the end: 96 rows over
-// 16 sequences of 8192 tokens, 8 heads, in 167 us (221 when one warpgroup worked alone).
+// 16 sequences of 8192 tokens, 8 heads, in 166 us (221 when one warpgroup worked alone).
 //   warps 10, 11 and 12, 15  converters of K and of V: 8-bit half tile -> fp16 (codes times
 //             factor) in the layout the products read; tokens past the end become zeros.
 // The line of tiles is divided over the pairs as kv_plan.cuh says; a run crosses units.

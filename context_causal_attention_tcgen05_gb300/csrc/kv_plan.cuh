@@ -7,8 +7,8 @@
 // into equal runs, one a CTA: no length or mask leaves an SM idle.  A unit takes some places
 // of the line before its first tile, which stand for the work around its tiles (its q, its
 // first maximum, its result): runs end together whether they cross few units or many (64
-// sequences of 750 to 3000 tokens, one row each, 58.3 us without such places, 55.6 so; three
-// prompts' chunks of 150 to 300 rows 107.6 and 99.9).  A unit inside one run
+// sequences of 750 to 3000 tokens, one row each, 54.9 us without such places, 52.3 so; three
+// prompts' chunks of 150 to 300 rows 103.8 and 96.8).  A unit inside one run
 // is written by its CTA; a unit cut between runs leaves per-row (m, l, O) in the
 // workspace, and kv_attn_join_kernel adds them in the runs' order, so results do not
 // depend on timing.
@@ -71,7 +71,7 @@ __device__ __forceinline__ void slot_seq(const CacheAttnArgs& a, const int32_t* 
   if (s.len != kl[b]) record_device_error(a.err, kDevIndex);
 }
 // Planning code runs once a unit and meets a cold instruction cache, so its largest part is
-// a function of its own (decoding one token over 1000: 10.5 us inlined everywhere, 10.0 us so).
+// a function of its own (decoding one token over 1000: 10.9 us inlined everywhere, 10.4 us so).
 // The rows kernel defines it inline: a call costs its register split.
 #ifndef KV_PLAN_INLINE
 #define KV_PLAN_INLINE __noinline__

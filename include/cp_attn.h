@@ -444,12 +444,15 @@ typedef struct {
  *   out [rows, Hq, D] in `dtype`, lse [Hq, rows] fp32; a row that sees no token has
  *   out = 0 and lse = -inf.  A row that sees any token of a block whose key or value
  *   scale is NaN gets NaN in out and lse.
- * Supported: Hq % Hkv == 0; D in {64, 128}; CP_F32 and CP_BF16.  Scores and sums are
- * fp32.  A row's weights are kept in steps of 2^-22 (bf16) or 2^-28 (fp32) of its own
- * largest product of a weight and a value scale, while the value scales that rows of
- * the call see lie within 2^40 of one another; CP_BF16 also rounds each to 11 bits
- * (2^-12 of itself).  workspace >= cp_workspace_size(CP_OP_KV_ATTENTION, rows, Hq, Hkv, D, dtype,
- * n_seqs, 0) bytes; calls that may overlap on the GPU need workspaces of their own. */
+ * Supported: Hq % Hkv == 0; D in {64, 128}; CP_F32 and CP_BF16; q and values of
+ * magnitudes below 2^90 (partial sums are fp32).
+ * Scores and sums are fp32; elements of q below 2^-13 of their row's largest are taken
+ * to 2^-21 of it (CP_F32 2^-37).  A row's weights are kept in steps of 2^-22 (CP_BF16)
+ * or 2^-28 (CP_F32) of its own largest product of a weight and a value scale, while the
+ * value scales that the call's rows see lie within 2^40 of one another; CP_BF16 also
+ * rounds each to 11 bits (2^-12 of itself).
+ *   workspace >= cp_workspace_size(CP_OP_KV_ATTENTION, rows, Hq, Hkv, D, dtype, n_seqs, 0)
+ *   bytes; calls that may overlap on the GPU need workspaces of their own. */
 CP_API cp_status cp_kv_cache_attention(const cp_kv_cache* cache, const void* q, int64_t rows,
                                        int64_t q_row_stride, int32_t Hq, int32_t dtype, const int32_t* cu_q,
                                        const int32_t* kv_len, const cp_cache_mask* mask, float scale,
@@ -494,7 +497,7 @@ CP_API cp_status cp_workspace_size(int32_t op, int64_t S, int32_t Hq, int32_t Hk
 
 /* Synchronises `stream`, then reports (and clears) the library's device error
  * word: CP_ERR_DEVICE_TIMEOUT if a kernel gave up on a bounded wait since the
- * last check, CP_ERR_DEVICE_INDEX if a debug build's index check failed,
+ * last check, CP_ERR_DEVICE_INDEX if an index check failed (see there),
  * CP_ERR_CUDA if the stream holds a CUDA error, else CP_OK. */
 CP_API cp_status cp_check_device_status(void* stream);
 
