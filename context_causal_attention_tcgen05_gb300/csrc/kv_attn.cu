@@ -7,9 +7,9 @@
 // are applied to scores and weights.  tcgen05's kind::f8f6f4 multiplies e4m3 exactly
 // and adds in fp32 (measured: 1e-8 relative, as an fp32 chain), so the other operand
 // is split into e4m3 parts: q = 2^e sum_i q_i 16^-i with q_i the e4m3
-// rounding of 16 times what the parts before it left, 2 parts for the 8 bits of bf16,
-// 6 for the 24 of fp32 (whole for elements down to 2^-13 of the row's largest; smaller ones
-// are off by up to 2^-21 and 2^-37 of it).  The weights of bf16 likewise, 3 parts of an 11-bit
+// rounding of 16 times what the parts before it left, 3 parts for the 8 bits of bf16,
+// 6 for the 24 of fp32 (whole for elements down to 2^-17 and 2^-13 of the row's largest;
+// smaller ones are off by up to 2^-25 and 2^-37 of it).  The weights of bf16 likewise, 3 parts of an 11-bit
 // rounding (fp16: 2^-12 of each, an eighth of half a step of a bf16 result; their sum is
 // kept whole); those of fp32 as 32-bit whole numbers in 8 parts of 4 bits: code k < 16 is k 2^-9 (subnormals
 // and the first binade are one line), so a digit is its own code and no conversion is needed.
@@ -78,7 +78,8 @@ struct Cfg {
   static constexpr int row_of(int c) { return NPP == 3 ? c % NR : c / 8 % NR; }
   static constexpr int kPitch = NO <= 32 ? 32 : (NO <= 64 ? 64 : 128);  // bytes of a token's weights
   static constexpr int kTile = BK * D;
-  static constexpr int kQBytes = NS * D;
+  // (a product of NS columns reads up to 8 rows behind its Q, of the next buffer: columns that nobody loads)
+  static constexpr int kQBytes = (RT * NPQ * D + 1023) / 1024 * 1024;
   static constexpr int kPBytes = BK * kPitch;
   static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 2048 + 1024;
   static constexpr int kBudget = 113 * 1024;  // two CTAs an SM
@@ -848,8 +849,8 @@ namespace {
 
 // Many rows a key: the rows kernel.  Its tile costs the same for 1 to 256 rows, this kernel's
 // grows by 16 rows (16 sequences of 8192 tokens, 8 heads of 128: 156 to 161 us for 16 to 64 rows
-// against 67 for 16, 123 for 32, 176 for 48, 224 for 64; D = 64: 135 to 141 us against 55, 89, 129 and
-// 159).
+// against 67 for 16, 124 for 32, 176 for 48, 225 for 64; D = 64: 135 to 141 us against 56, 90, 129 and
+// 161).
 bool many_rows(int64_t rows, int64_t G, int64_t n_seqs, bool is_bf16) { return is_bf16 && rows * G > 32 * n_seqs; }
 
 }  // namespace
@@ -868,13 +869,13 @@ cp_status launch_kv_attention(const CacheAttnArgs& a, int is_bf16, void* ws, cud
   if (a.D == 128) {
     if (!is_bf16)
       return rows <= 4 * n ? launch_cfg<Cfg<128, 4, 6, 8, 1>, false>(a, ws, st) : launch_cfg<Cfg<128, 8, 6, 8, 2>, false>(a, ws, st);
-    if (rows <= 4 * n) return launch_cfg<Cfg<128, 4, 2, 3, 1>, true>(a, ws, st);
-    return rows <= 8 * n ? launch_cfg<Cfg<128, 8, 2, 3, 1>, true>(a, ws, st) : launch_cfg<Cfg<128, 16, 2, 3, 1>, true>(a, ws, st);
+    if (rows <= 4 * n) return launch_cfg<Cfg<128, 4, 3, 3, 1>, true>(a, ws, st);
+    return rows <= 8 * n ? launch_cfg<Cfg<128, 8, 3, 3, 1>, true>(a, ws, st) : launch_cfg<Cfg<128, 16, 3, 3, 1>, true>(a, ws, st);
   }
   if (!is_bf16)
     return rows <= 4 * n ? launch_cfg<Cfg<64, 4, 6, 8, 1>, false>(a, ws, st) : launch_cfg<Cfg<64, 8, 6, 8, 2>, false>(a, ws, st);
-  if (rows <= 4 * n) return launch_cfg<Cfg<64, 4, 2, 3, 1>, true>(a, ws, st);
-  return rows <= 8 * n ? launch_cfg<Cfg<64, 8, 2, 3, 1>, true>(a, ws, st) : launch_cfg<Cfg<64, 16, 2, 3, 1>, true>(a, ws, st);
+  if (rows <= 4 * n) return launch_cfg<Cfg<64, 4, 3, 3, 1>, true>(a, ws, st);
+  return rows <= 8 * n ? launch_cfg<Cfg<64, 8, 3, 3, 1>, true>(a, ws, st) : launch_cfg<Cfg<64, 16, 3, 3, 1>, true>(a, ws, st);
 }
 
 }  // namespace cpa

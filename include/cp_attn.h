@@ -446,8 +446,8 @@ typedef struct {
  *   scale is NaN gets NaN in out and lse.
  * Supported: Hq % Hkv == 0; D in {64, 128}; CP_F32 and CP_BF16; q and values of
  * magnitudes below 2^90 (partial sums are fp32).
- * Scores and sums are fp32; elements of q below 2^-13 of their row's largest are taken
- * to 2^-21 of it (CP_F32 2^-37).  A row's weights are kept in steps of 2^-22 (CP_BF16)
+ * Scores and sums are fp32; elements of q below 2^-17 of their row's largest are taken
+ * to 2^-25 of it (CP_F32: below 2^-13, to 2^-37).  A row's weights are kept in steps of 2^-22 (CP_BF16)
  * or 2^-28 (CP_F32) of its own largest product of a weight and a value scale, while the
  * value scales that the call's rows see lie within 2^40 of one another; CP_BF16 also
  * rounds each to 11 bits (2^-12 of itself).

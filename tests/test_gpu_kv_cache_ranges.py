@@ -238,3 +238,27 @@ def test_errors_in_the_2_norm(n, dtype, D):
         assert e <= bound
         assert np.abs(lse[:, rows].double().cpu().numpy() - rl).max() <= 2.0**-17 * max(1, np.abs(rl).max())
     check_ok()
+
+
+@pytest.mark.parametrize("n,dtype", [(1, BF16), (2, BF16), (4, BF16), (40, BF16), (1, F32), (6, F32)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_query_element_that_dwarfs_the_others(n, dtype, D):
+    """The first element of every query row is 2^14 times as large as the others, and the keys are zero there: scores are
+    made of the others alone."""
+    L = 500
+    c = Cache([L], 2, D, 32)
+    k, v = randn(L, 2, D, dtype=F32), randn(L, 2, D, dtype=F32, seed=1)
+    k[..., 0] = 0
+    c.append(k, v, [L], [0], check=False)
+    q = randn(n, 8, D, dtype=F32, seed=2)
+    q[..., 0] = 2.0**14
+    q = q.to(dtype)
+    out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32([L]), i32([0, n]))
+    ref, rl, bo, bl = reference(c, 0, q, L, np.arange(L - n, L))
+    absv = serving.cache_attention(q.double().cpu().numpy(), c.values(0, 0, L), c.values(1, 0, L), np.arange(L - n, L), np.arange(L))[2]
+    # elements of q from 2^-17 of the row's largest on are whole, smaller ones within 2^-25 of it (fp32 2^-13, 2^-37)
+    x = np.abs(q.double().cpu().numpy())
+    lost = (x < (2.0**-17 if dtype == BF16 else 2.0**-13) * 2.0**14) * (2.0**-25 if dtype == BF16 else 2.0**-37) * 2.0**14
+    ds = np.stack([(lost[:, h] @ np.abs(c.values(0, 0, L)[:, h // 4]).T).max(axis=1) for h in range(8)], axis=1) * D**-0.5
+    check_rows(out, lse, ref, rl, bo + 2 * ds[:, :, None] * (absv + np.abs(ref)), bl + ds.T, what=f"large element {n}")
+    check_ok()
