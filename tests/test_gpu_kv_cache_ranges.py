@@ -262,3 +262,30 @@ def test_a_query_element_that_dwarfs_the_others(n, dtype, D):
     ds = np.stack([(lost[:, h] @ np.abs(c.values(0, 0, L)[:, h // 4]).T).max(axis=1) for h in range(8)], axis=1) * D**-0.5
     check_rows(out, lse, ref, rl, bo + 2 * ds[:, :, None] * (absv + np.abs(ref)), bl + ds.T, what=f"large element {n}")
     check_ok()
+
+
+@pytest.mark.parametrize("n,dtype", [(3, BF16), (40, BF16), (200, BF16), (300, BF16), (3, F32)])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_nan_blocks_and_bad_pages_among_scales_far_apart(where, n, dtype):
+    """Keys and values that differ by 2^20 from page to page, a page that does not exist and a NaN block: the tokens of the
+    first are hidden, the second reaches the rows that see it alone."""
+    L, page = 700, 16
+    c = Cache([L], 2, 64, page)
+    mag = torch.exp2((torch.arange(L, device="cuda") // page * 7 % 21).float())[:, None, None]
+    c.append(randn(L, 2, 64, dtype=F32) / mag, randn(L, 2, 64, dtype=F32, seed=1) * mag, [L], [0], check=False)
+    i, late = "kv".index(where), int(c.table[0, 43])  # tokens 688 on, head 1
+    c.t[2 + i][late, 1] = float("nan")
+    c.t[4][0, 5] = -1
+    pos = np.where(np.arange(n) % 2 == 0, 687 - np.arange(n) // 2, 699)
+    q = randn(n, 8, 64, dtype=dtype, seed=2)
+    out, lse = cpa.cp_kv_cache_attention(q, *c.args(), i32([L]), i32([0, n]), q_pos=i32(pos))
+    assert cpa.cp_check_device_status() == -9
+    hit = torch.from_numpy(pos >= 688).cuda()
+    assert torch.isnan(out[hit][:, 4:]).all() and torch.isnan(lse[4:, hit]).all()
+    assert torch.isfinite(out[hit][:, :4]).all() and torch.isfinite(lse[:4, hit]).all()
+    keep = np.array([t for t in range(L) if t // page != 5])
+    scale = c.scales[1][[int(c.table[0][t // page]) for t in keep]].astype(np.float64)
+    ref = reference(c, 0, q, L, pos, pos_k=keep, k=c.values(0, 0, L)[keep], v=c.values(1, 0, L)[keep], v_scale=scale)
+    ok = ~hit.cpu().numpy()
+    check_rows(out[~hit], lse[:, ~hit], ref[0][ok], ref[1][:, ok], ref[2][ok], ref[3][:, ok], what=f"far apart {n}")
+    check_ok()
